@@ -151,7 +151,7 @@ la_status run_step(Args a, int B, cudaStream_t stream) {
 
 template <typename T, int KD, int RT, int NBUF>
 la_status run_chunks(Args a, int B, cudaStream_t stream) {
-  constexpr int PC = kChainPlanes, PO = out_planes<T>();
+  constexpr int PC = kChainPlanes, PO = kChainPlanes;
   const long long heads = (long long)B * a.H;
   const la_status st = run_terms<T, KD, PC, PO>(a, heads, stream);
   if (st != LA_OK) return st;
@@ -192,9 +192,7 @@ la_status run_forward(const Args& a, int B, bool is_bf16, bool few, cudaStream_t
 size_t forward_bytes(const la_delta_params& p) {
   if (few_tokens(p)) return 0;
   const size_t chunks = (size_t)p.B * p.H * ((p.N + kC - 1) / kC);
-  return LA_WORKSPACE_CONTROL_BYTES +
-         chunks * (p.dtype == LA_BF16 ? Record<kChainPlanes, out_planes<bf16>()>::bytes
-                                      : Record<kChainPlanes, out_planes<float>()>::bytes);
+  return LA_WORKSPACE_CONTROL_BYTES + chunks * Record<kChainPlanes, kChainPlanes>::bytes;
 }
 
 }  // namespace

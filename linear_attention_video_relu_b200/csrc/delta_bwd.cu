@@ -1252,7 +1252,7 @@ struct BwdBytes {
   int atoms;
   explicit BwdBytes(const la_delta_params& p) {
     const size_t heads = (size_t)p.B * p.H, chunks = heads * ((p.N + kC - 1) / kC);
-    const size_t po = p.dtype == LA_BF16 ? out_planes<bf16>() : out_planes<float>();
+    const size_t po = p.dtype == LA_BF16 ? grad_planes<bf16>() : grad_planes<float>();
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     atoms = (p.Dv + 63) / 64;
     rec = up(chunks * Record<kChainPlanes, kChainPlanes>::bytes);
@@ -1265,7 +1265,7 @@ struct BwdBytes {
 
 template <typename T, int KD, int RT, int PC, int NBUF, int GNV = 16>
 la_status run_backward(Args a, int B, cudaStream_t stream) {
-  constexpr int PO = out_planes<T>();
+  constexpr int PO = grad_planes<T>();
   const long long heads = (long long)B * a.H;
   la_status st = run_terms<T, KD, PC, PC>(a, heads, stream);
   if (st != LA_OK) return st;

@@ -92,11 +92,11 @@ inline la_status wide_chains(long long heads, int Dv, bool* wide) {
   return LA_OK;
 }
 
-// Planes of what the carried state is made from (all bits of fp32), and of
-// what only the outputs are made from.
+// Planes of what the carried state and the outputs are made from (all bits of
+// fp32), and of what only gradients in T are made from.
 constexpr int kChainPlanes = 3;
 template <typename T>
-constexpr int out_planes() { return sizeof(T) == 2 ? 2 : 3; }
+constexpr int grad_planes() { return sizeof(T) == 2 ? 2 : 3; }
 
 template <typename T, int KD, int PC, int PO>
 la_status run_terms(const Args& a, long long heads, cudaStream_t stream) {

@@ -21,10 +21,13 @@
 // of the chain can begin, and its operands, three planes of 128 x 128 state,
 // would leave shared memory no room for the next chunk's.
 //
-// Rounding: the state, T, R and X enter products as PC bf16 planes (three: all
-// bits of fp32), so the carried state loses nothing to the tensor cores; what
-// only `out` needs (Q S, P X) takes PO planes (two for bf16 out: 17 bits, then
-// one rounding to 8).
+// Rounding: the state, T, R and X enter products as PC bf16 planes, and what only
+// the outputs or gradients need (S beside Q, X beside P) as PO. Forward both are
+// three, all bits of fp32, so neither the carried state nor `out` loses anything
+// to the tensor cores: of outputs in bf16 0.012 % are not the rounding of the
+// exact value, as of an fp32 computation (four heads of 1024 tokens, D 64). With
+// PO = 2, 17 bits, that is 0.76 %, for 6 to 9 % less time (480p clip 930 us
+// and 992, ragged batch 577 and 629, D 112 block 171 and 181).
 #pragma once
 
 #include "delta.cuh"
