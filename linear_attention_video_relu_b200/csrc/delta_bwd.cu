@@ -11,10 +11,12 @@
 //     dq   = w . (dO S^T) + EP K                        EP = scale E . dP
 //     dk   = z . (X dS'^T) - x . (dR S^T) + EP^T Q + (F + F^T) K,  F = beta E . dA
 //     dbeta_i = dR_i.(v_i - e_i S^T k_i) + sum_j E_ij dA_ij k_i.k_j
-//     dG_i = q_i.(w . dO S^T)_i - k_i.(x . dR S^T)_i - k_i.(z . X dS'^T)_i
-//            + sum_j (dP.P + dA.A)_ij - sum_j (dP.P + dA.A)_ji
-//     dG_last += exp(G_last) <S, dS'> + sum_i k_i.(z . X dS'^T)_i
-//     dg_i = sum of dG_j over the chunk's j >= i.
+//     dg_t = exp(G_last) <S, dS'> + sum_{i >= t} (q_i.(w . dO S^T)_i - k_i.(x . dR S^T)_i)
+//            + sum_{j < t} k_j.(z . X dS'^T)_j + sum_{i >= t > j} M_ij,   M = dP.P + dA.A.
+// (dg is that of the sums G, summed from t on: of what a pair or a row has in it,
+// the terms whose decay does not pass t cancel. They are left out here, so that
+// every term of dg_t has exp(g_t) in it, and a decay that forgets nearly all
+// has a gradient with digits of its own and not the others' rounding.)
 // Nothing is kept from the forward pass: the states before the chunks are made
 // again (scan_kernel), then the gradients of the states are carried backwards
 // (reverse_kernel), and with both in the workspace all chunks' gradients are
@@ -416,8 +418,9 @@ struct Within {
   const Gates* gates;
   const Decays* dec;
   // sums of rows, by quarter of the columns: [0 ..] q.dq, [4 ..] k.ki, [8 ..]
-  // k.ko, [12 ..] dP.P + dA.A along rows, [20 ..] for dbeta; [16 ..] dP.P + dA.A
-  // along columns, by row tile; [24] dR.v; then <S, dS'> by warp
+  // k.ko, [12 ..] M along rows, [20 ..] for dbeta; [16 ..] M along columns, by row
+  // tile; [24] dR.v; then <S, dS'> by warp. Of a diagonal block M's row sums give
+  // way to what dg takes of it, sum_{i >= t > j} M_ij by t.
   float* sums;
 };
 
@@ -449,6 +452,7 @@ __device__ __forceinline__ void make_within(const Within& x, float scale,
   float* sums = x.sums;
   if (ch <= m) {
     float row_sum[2] = {0.f, 0.f}, beta_sum[2] = {0.f, 0.f};
+    float M[2][2][2];   // of a diagonal block: column tile, row, column
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const int cc = 8 * n + c2, col = 16 * ch + cc;
@@ -469,6 +473,7 @@ __device__ __forceinline__ void make_within(const Within& x, float scale,
           const float kk = acc[0][n][2 * i + e];
           f[e] = bt * ea;
           const float mix = (in ? ep[e] * acc[1][n][2 * i + e] : 0.f) + (below ? f[e] * kk : 0.f);
+          M[n][i][e] = mix;
           row_sum[i] += mix;
           col_sum[e] += mix;
           if (below) beta_sum[i] += ea * kk;
@@ -485,6 +490,26 @@ __device__ __forceinline__ void make_within(const Within& x, float scale,
         y += __shfl_xor_sync(0xffffffffu, y, 16);
         if (r == 0) sums[(16 + m) * kC + col + e] = y;
       }
+    }
+    if (ch == m) {
+      // sum over the rows from t on, then over the columns before t
+      row_sum[0] = row_sum[1] = 0.f;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float lo = M[n][0][e], hi = M[n][1][e];   // rows r and r + 8
+#pragma unroll
+          for (int o = 4; o < 32; o *= 2) {
+            const float u = __shfl_down_sync(0xffffffffu, lo, o);
+            const float v = __shfl_down_sync(0xffffffffu, hi, o);
+            if (lane + o < 32) lo += u, hi += v;
+          }
+          lo += __shfl_sync(0xffffffffu, hi, lane & 3);
+          const int cc = 8 * n + c2 + e;
+          if (cc < r) row_sum[0] += lo;
+          if (cc < r + 8) row_sum[1] += hi;
+        }
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -591,44 +616,85 @@ __device__ __forceinline__ void finish(const Args& a, const Within& x, int bh, i
 
   // dbeta and dg: one warp, lane l has tokens 2l and 2l + 1
   if (warp == 0) {
-    float dG[2], out = 0.f;
+    float in[2], out[2], row[2], col[2];
+    const int tile = lane >> 3;
     const Rows rg = rows_of(a, b, h, a.H, 1);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int i = 2 * lane + e;
       const float4 g = gates->tok[i];
-      float y[6];   // the six sums of the token, each over four parts
+      float y[4];   // four sums of the token, each over four parts
 #pragma unroll
-      for (int j = 0; j < 6; ++j)
-        y[j] = (sums[4 * j * kC + i] + sums[(4 * j + 1) * kC + i]) +
-               (sums[(4 * j + 2) * kC + i] + sums[(4 * j + 3) * kC + i]);
-      const float kod = g.z * y[2];
-      dG[e] = g.w * y[0] - g.x * y[1] - kod + y[3] - y[4];
-      out += kod;
+      for (int j = 0; j < 4; ++j) {
+        const float* s = sums + (j == 3 ? 20 : 4 * j) * kC + i;
+        y[j] = (s[0] + s[kC]) + (s[2 * kC] + s[3 * kC]);
+      }
+      in[e] = g.w * y[0] - g.x * y[1];
+      out[e] = g.z * y[2];
       if (i < rows) {
-        const float db = sums[24 * kC + i] - expf((float)dec->G[i]) * y[1] + y[5];
+        const float db = sums[24 * kC + i] - expf((float)dec->G[i]) * y[1] + y[3];
         mm::Io<T>::store(static_cast<T*>(a.dbeta) + rg.base + (t0 + i) * rg.stride, db);
       }
-    }
+      // of the blocks left of the diagonal one in this row tile, and of those
+      // below it in this column tile
+      row[e] = col[e] = 0.f;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) out += __shfl_xor_sync(0xffffffffu, out, o);
+      for (int j = 0; j < 3; ++j) {
+        if (j < tile) row[e] += sums[(12 + j) * kC + i];
+        if (3 - j > tile) col[e] += sums[(16 + 3 - j) * kC + i];
+      }
+    }
+    // what lies below this tile's row and left of its column: the blocks (2, 0)
+    // and (3, 0) for tile 1, (3, 0) and (3, 1) for tile 2
+    float part[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      part[j] = sums[(12 + j) * kC + 2 * lane] + sums[(12 + j) * kC + 2 * lane + 1];
+#pragma unroll
+      for (int o = 1; o < 8; o *= 2) part[j] += __shfl_xor_sync(0xffffffffu, part[j], o);
+    }
+    const float b20 = __shfl_sync(0xffffffffu, part[0], 16);
+    const float b30 = __shfl_sync(0xffffffffu, part[0], 24);
+    const float b31 = __shfl_sync(0xffffffffu, part[1], 24);
     float dot = 0.f;
     for (int j = 0; j < 16; ++j) dot += sums[25 * kC + j];
-    const float end = gates->last[0] * dot + out;
-    // suffix sums
-    float t = dG[0] + dG[1];
+    float end = gates->last[0] * dot;
+    if (tile == 1) end += b20 + b30;
+    if (tile == 2) end += b30 + b31;
+    // sums over the tokens from this lane's on, of `in` to the chunk's end and of
+    // `row` to the tile's; and over those before it
+    float in_t = in[0] + in[1], row_t = row[0] + row[1];
+    float out_t = out[0] + out[1], col_t = col[0] + col[1];
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-      const float u = __shfl_down_sync(0xffffffffu, t, o);
-      if (lane + o < 32) t += u;
+      const float u = __shfl_down_sync(0xffffffffu, in_t, o);
+      const float v = __shfl_up_sync(0xffffffffu, out_t, o);
+      if (lane + o < 32) in_t += u;
+      if (lane >= o) out_t += v;
+      if (o < 8) {
+        const float w = __shfl_down_sync(0xffffffffu, row_t, o, 8);
+        const float z = __shfl_up_sync(0xffffffffu, col_t, o, 8);
+        if ((lane & 7) + o < 8) row_t += w;
+        if ((lane & 7) >= o) col_t += z;
+      }
     }
-    const float after = t - (dG[0] + dG[1]);
+    // without this lane's own two tokens
+    float after = __shfl_down_sync(0xffffffffu, in_t, 1);
+    float rest = __shfl_down_sync(0xffffffffu, row_t, 1, 8);
+    float before = __shfl_up_sync(0xffffffffu, out_t, 1);
+    float left = __shfl_up_sync(0xffffffffu, col_t, 1, 8);
+    if (lane == 31) after = 0.f;
+    if ((lane & 7) == 7) rest = 0.f;
+    if (lane == 0) before = 0.f;
+    if ((lane & 7) == 0) left = 0.f;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int i = 2 * lane + e;
+      float dg = e == 0 ? (in_t + before) + (row_t + left)
+                        : (after + in[1] + before + out[0]) + (rest + row[1] + left + col[0]);
+      dg += end + sums[(12 + tile) * kC + i];
       if (i < rows)
-        mm::Io<T>::store(static_cast<T*>(a.dg) + rg.base + (t0 + i) * rg.stride,
-                         end + (e == 0 ? t : after + dG[1]));
+        mm::Io<T>::store(static_cast<T*>(a.dg) + rg.base + (t0 + i) * rg.stride, dg);
     }
   }
 }
