@@ -99,6 +99,13 @@ def _on_stream(t: torch.Tensor, stream: Optional[torch.cuda.Stream]):
     return torch.cuda.stream(stream)
 
 
+def _int32(x, what):
+    """x, which the C side's int has to hold (ctypes would cut it off)."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError("%s must fit a 32-bit int, got %s" % (what, x))
+    return x
+
+
 _DTYPE_OF = {v: k for k, v in _DTYPES.items()}
 
 
@@ -552,15 +559,16 @@ def _rotary(q, k, positions, offset, grid, rope_split, dim, style, theta, scalin
         raise ValueError("scaling must be 'none', 'linear', 'ntk' or 'by_parts'")
     if (grid is None) != (rope_split is None):
         raise ValueError("grid and rope_split go together")
-    p = C.la_rotary_params(B, H, 0, N, D, D if dim is None else dim, _DTYPES[dt],
+    offset, dim_ = _int32(offset, "offset"), D if dim is None else _int32(dim, "dim")
+    p = C.la_rotary_params(B, H, 0, N, D, dim_, _DTYPES[dt],
                            _LAYOUTS[layout], _STYLES[style], _SCALINGS[scaling], transpose, 0,
                            offset, 0, 0, 0, 0, 0, 0, theta, factor, original_length, low, high,
                            amplitude)
     if grid is not None:
         if positions is not None:
             raise ValueError("positions and grid exclude each other")
-        p.grid_t, p.grid_h, p.grid_w = (int(x) for x in grid)
-        p.rope_dt, p.rope_dh, p.rope_dw = (int(x) for x in rope_split)
+        p.grid_t, p.grid_h, p.grid_w = (_int32(int(x), "grid") for x in grid)
+        p.rope_dt, p.rope_dh, p.rope_dw = (_int32(int(x), "rope_split") for x in rope_split)
         if dim is None:
             p.dim = p.rope_dt + p.rope_dh + p.rope_dw
     if not (dev >= 0 and q.is_contiguous()):
