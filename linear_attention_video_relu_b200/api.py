@@ -262,6 +262,7 @@ class BlockState:
              grid=None, rope_split=None, theta: float = 10000.0, eps: float = 1e-6,
              out=None, stream=None, layout: str = "bhnd") -> torch.Tensor:
         """One block of block-causal attention against the carried state."""
+        _int32(t_offset, "t_offset")
         p, ws = self._plan(q, grid, rope_split, theta, eps, layout)
         _check_io(p, q, k, v, gate)
         if out is None:
@@ -280,6 +281,7 @@ class BlockState:
     def update(self, k, v, *, t_offset: int = 0, grid=None, rope_split=None,
                theta: float = 10000.0, stream=None, layout: str = "bhnd") -> None:
         """Fold a block's k, v into the state without producing output."""
+        _int32(t_offset, "t_offset")
         p, ws = self._plan(k, grid, rope_split, theta, 1e-6, layout)
         _check_io(p, k, v)
         _same_device(self.S, k, v)

@@ -1,5 +1,5 @@
-"""Rotary arguments that no 32-bit int holds are refused, not cut off to one that
-another call could have meant."""
+"""Positions and sizes that no 32-bit int holds are refused, not cut off to one
+that another call could have meant."""
 import pytest
 import torch
 
@@ -14,3 +14,13 @@ import linear_attention_video_relu_b200 as la
 def test_values_past_32_bits(call, bad):
     with pytest.raises(ValueError, match="32-bit"):
         call(torch.zeros(1, 2, 8, 64), **bad)
+
+
+@pytest.mark.parametrize("bad", [2 ** 32 + 5, 2 ** 31])
+def test_block_offsets_past_32_bits(bad):
+    st = object.__new__(la.BlockState)   # refused before anything of it is read
+    x = torch.zeros(1, 2, 8, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="32-bit"):
+        st.step(x, x, x, t_offset=bad)
+    with pytest.raises(ValueError, match="32-bit"):
+        st.update(x, x, t_offset=bad)
