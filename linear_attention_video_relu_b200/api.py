@@ -81,22 +81,24 @@ _same = contextlib.nullcontext()
 
 
 def _on_device(t: torch.Tensor):
-    """t's device made current for the call; no switch when it already is."""
+    """t's device made current for the call; no switch when it already is, nor for
+    host tensors (which the checks of the call refuse)."""
     idx = t.get_device()
-    if idx == _current_device():
+    if idx < 0 or idx == _current_device():
         return _same
     return torch.cuda.device(idx)
 
 
-def _on_stream(t: torch.Tensor, stream: Optional[torch.cuda.Stream]):
-    """_on_device(t) for a call that also makes its results and its workspace:
+def _on_stream(t: torch.Tensor, stream: Optional[torch.cuda.Stream], makes: bool = True):
+    """_on_device(t) for a call that also makes its results or its workspace:
     with a stream given, that is current for the call, so that they are filled
-    on it and the allocator hands their memory on in its order."""
+    on it and the allocator hands their memory on in its order. A call that
+    `makes` nothing need not switch."""
     if stream is None:
         return _on_device(t)
     if stream.device != t.device:
         raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
-    return torch.cuda.stream(stream)
+    return torch.cuda.stream(stream) if makes else _on_device(t)
 
 
 def _int32(x, what):
@@ -174,13 +176,13 @@ def forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gate: Optional[to
     p = make_params(B, H, N, D, q.dtype, mode, block_tokens, grid, rope_split, theta, eps,
                     layout)
     _check_io(p, q, k, v, gate)
-    if out is None:
-        out = torch.empty_like(q)
-    _check_io(p, out)
-    _same_device(q, k, v, gate, out, None if workspace is None else workspace.buf)
-    if workspace is None:
-        workspace = workspace_for(p, q.device)
-    with _on_device(q):
+    with _on_stream(q, stream, out is None or workspace is None):
+        if out is None:
+            out = torch.empty_like(q)
+        _check_io(p, out)
+        _same_device(q, k, v, gate, out, None if workspace is None else workspace.buf)
+        if workspace is None:
+            workspace = workspace_for(p, q.device)
         C.check(C.lin_attn_forward(p, _ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(out),
                                    workspace.ptr, workspace.nbytes,
                                    _stream(stream, q.get_device())), "lin_attn_forward")
@@ -202,14 +204,13 @@ def cross_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     pk = make_params(B, H, M, D, q.dtype, eps=eps, layout=layout)
     _check_io(p, q, gate)
     _check_io(pk, k, v)
-    if out is None:
-        out = torch.empty_like(q)
-    _check_io(p, out)
-    _same_device(q, k, v, gate, out, None if workspace is None else workspace.buf)
-    if workspace is None:
-        with torch.cuda.device(q.device):
+    with _on_stream(q, stream, out is None or workspace is None):
+        if out is None:
+            out = torch.empty_like(q)
+        _check_io(p, out)
+        _same_device(q, k, v, gate, out, None if workspace is None else workspace.buf)
+        if workspace is None:
             workspace = Workspace(C.lin_attn_cross_workspace_size(p, M), q.device)
-    with _on_device(q):
         C.check(C.lin_attn_cross_forward(p, M, _ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(out),
                                          workspace.ptr, workspace.nbytes,
                                          _stream(stream, q.get_device())),
@@ -263,15 +264,15 @@ class BlockState:
              out=None, stream=None, layout: str = "bhnd") -> torch.Tensor:
         """One block of block-causal attention against the carried state."""
         _int32(t_offset, "t_offset")
-        p, ws = self._plan(q, grid, rope_split, theta, eps, layout)
-        _check_io(p, q, k, v, gate)
-        if out is None:
-            out = torch.empty_like(q)
-        else:
-            _check_io(p, out)
-        _same_device(self.S, q, k, v, gate, out)
-        dev = q.get_device()
-        with _on_device(q):
+        with _on_stream(self.S, stream):
+            p, ws = self._plan(q, grid, rope_split, theta, eps, layout)
+            _check_io(p, q, k, v, gate)
+            if out is None:
+                out = torch.empty_like(q)
+            else:
+                _check_io(p, out)
+            _same_device(self.S, q, k, v, gate, out)
+            dev = q.get_device()
             C.check(C.lin_attn_block_step(p, self._st, t_offset, q.data_ptr(), k.data_ptr(),
                                           v.data_ptr(), _ptr(gate), out.data_ptr(),
                                           1 if commit else 0, ws.ptr, ws.nbytes,
@@ -282,10 +283,10 @@ class BlockState:
                theta: float = 10000.0, stream=None, layout: str = "bhnd") -> None:
         """Fold a block's k, v into the state without producing output."""
         _int32(t_offset, "t_offset")
-        p, ws = self._plan(k, grid, rope_split, theta, 1e-6, layout)
-        _check_io(p, k, v)
-        _same_device(self.S, k, v)
-        with _on_device(k):
+        with _on_stream(self.S, stream):
+            p, ws = self._plan(k, grid, rope_split, theta, 1e-6, layout)
+            _check_io(p, k, v)
+            _same_device(self.S, k, v)
             C.check(C.lin_attn_state_update(p, self._st, t_offset, k.data_ptr(), v.data_ptr(),
                                             ws.ptr, ws.nbytes, _stream(stream, k.get_device())),
                     "lin_attn_state_update")
@@ -316,23 +317,23 @@ def temporal_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Te
     for d in x.shape[2:-1]:
         S *= int(d)
     frame_shape = (B,) + tuple(x.shape[2:])
-    if out is None:
-        out = torch.empty_like(x)
-    for t, shape, dt, what in ((x, tuple(x.shape), x.dtype, "x"),
-                               (out, tuple(x.shape), x.dtype, "out"),
-                               (weight, (3, nc), torch.float32, "weight"),
-                               (bias, (nc,), torch.float32, "bias"),
-                               (cache_in, frame_shape, x.dtype, "cache_in"),
-                               (cache_out, frame_shape, x.dtype, "cache_out")):
-        if t is None:
-            continue
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous CUDA tensor" % what)
-        if tuple(t.shape) != shape or t.dtype != dt:
-            raise ValueError("%s must be %s %s, got %s %s" % (what, shape, dt, tuple(t.shape),
-                                                            t.dtype))
-    _same_device(x, out, weight, bias, cache_in, cache_out)
-    with torch.cuda.device(x.device):
+    with _on_stream(x, stream, out is None):
+        if out is None:
+            out = torch.empty_like(x)
+        for t, shape, dt, what in ((x, tuple(x.shape), x.dtype, "x"),
+                                   (out, tuple(x.shape), x.dtype, "out"),
+                                   (weight, (3, nc), torch.float32, "weight"),
+                                   (bias, (nc,), torch.float32, "bias"),
+                                   (cache_in, frame_shape, x.dtype, "cache_in"),
+                                   (cache_out, frame_shape, x.dtype, "cache_out")):
+            if t is None:
+                continue
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError("%s must be a contiguous CUDA tensor" % what)
+            if tuple(t.shape) != shape or t.dtype != dt:
+                raise ValueError("%s must be %s %s, got %s %s" % (what, shape, dt, tuple(t.shape),
+                                                                t.dtype))
+        _same_device(x, out, weight, bias, cache_in, cache_out)
         C.check(C.lin_attn_temporal_conv(B, T, S, nc, _DTYPES[x.dtype], _ptr(x), _ptr(weight),
                                          _ptr(bias), _ptr(cache_in), _ptr(out), _ptr(cache_out),
                                          _stream(stream)),
