@@ -1282,7 +1282,7 @@ __global__ void __launch_bounds__(512, 1) gradient_tc_kernel(const Args a) {
 }
 
 // dq and dk of shared heads: the sum over the value heads of a group, in their
-// order. Eight columns of a row per thread.
+// order (a group of none: zeros). Eight columns of a row per thread.
 template <typename T>
 __global__ void __launch_bounds__(256) shared_heads_kernel(const Args a) {
   ptx::grid_dependency_wait();
@@ -1329,6 +1329,12 @@ struct BwdBytes {
   }
 };
 
+template <typename T>
+la_status run_shared_heads(const Args& a, bool next, cudaStream_t stream) {
+  const long long count = (long long)a.B * a.Hk * a.N * (a.D / 8);
+  return launch<shared_heads_kernel<T>>((unsigned)((count + 255) / 256), 256, 0, stream, a, next);
+}
+
 template <typename T, int KD, int RT, int PC, int NBUF, int GNV = 16>
 la_status run_backward(Args a, int B, cudaStream_t stream) {
   constexpr int PO = grad_planes<T>();
@@ -1361,8 +1367,7 @@ la_status run_backward(Args a, int B, cudaStream_t stream) {
     st = launch<gradient_kernel<T, KD, GNV, PC, PO, 1>>(each, Grad::threads, Grad::bytes, stream, a, true);
   }
   if (st != LA_OK || a.Hk == a.H) return st;
-  const long long count = (long long)B * a.Hk * a.N * (a.D / 8);
-  return launch<shared_heads_kernel<T>>((unsigned)((count + 255) / 256), 256, 0, stream, a, true);
+  return run_shared_heads<T>(a, true, stream);
 }
 
 }  // namespace
@@ -1390,13 +1395,28 @@ la_status lin_attn_delta_backward(const la_delta_params* p, const void* dout, co
   la_status st = check_delta(p);
   if (st != LA_OK) return st;
   const long long heads = (long long)p->B * p->H;
-  if (heads == 0) return LA_OK;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (heads == 0) {
+    // without value heads, dq and dk are sums over none
+    const size_t n = DeltaBytes(*p).qk, nl = p->B * sizeof(int);
+    if (n == 0) return LA_OK;
+    if (!dq || !dk || !aligned16(dq) || !aligned16(dk) || !aligned(lengths, 4))
+      return LA_ERR_INVALID_ARG;
+    for (const void* in : {q, k})
+      if (overlaps(dq, n, in, n) || overlaps(dk, n, in, n)) return LA_ERR_INVALID_ARG;
+    if (overlaps(dq, n, dk, n) || overlaps(dq, n, lengths, nl) || overlaps(dk, n, lengths, nl))
+      return LA_ERR_INVALID_ARG;
+    Args a = delta_args(*p, q, k, v, log_decay, beta, state, lengths);
+    a.dq = dq;
+    a.dk = dk;
+    return p->dtype == LA_F32 ? run_shared_heads<float>(a, false, cs)
+                              : run_shared_heads<bf16>(a, false, cs);
+  }
   const size_t sbytes = (size_t)heads * p->D * p->Dv * sizeof(float);
   if (!aligned16(state) || !aligned16(dstate_out) || !aligned16(dstate)) return LA_ERR_INVALID_ARG;
   if (dstate && dstate != dstate_out && overlaps(dstate, sbytes, dstate_out, sbytes))
     return LA_ERR_INVALID_ARG;
   if (overlaps(dstate, sbytes, state, sbytes)) return LA_ERR_INVALID_ARG;
-  cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (p->N == 0) {
     if (!dstate || dstate == dstate_out) return LA_OK;
     const cudaError_t e =
