@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const Args a) {
   const bool in = col < a.Dv;
   const int len = length_of(a, b);
   const long long s_at = (long long)bh * a.D * a.Dv + col;
+  if (a.flag && blockIdx.x == 0 && threadIdx.x == 0) *a.flag = 0;   // nothing waits here
 
   float4 s[RPT];
 #pragma unroll
@@ -226,13 +227,9 @@ la_status lin_attn_delta_forward(const la_delta_params* p, const void* q, const 
     return LA_ERR_INVALID_ARG;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (p->N == 0) {
-    if (!state_out || state == state_out) return LA_OK;
-    const cudaError_t e =
-        state ? cudaMemcpyAsync(state_out, state, sbytes, cudaMemcpyDeviceToDevice, cs)
-              : cudaMemsetAsync(state_out, 0, sbytes, cs);
-    if (e == cudaSuccess) return LA_OK;
-    cudaGetLastError();
-    return LA_ERR_CUDA;
+    if (overlaps(flag_of(workspace, workspace_bytes), sizeof(int), state_out, sbytes))
+      return LA_ERR_INVALID_ARG;
+    return copy_state(state_out, state, sbytes, workspace, workspace_bytes, cs);
   }
   const DeltaBytes n(*p);
   const void* in[6] = {q, k, v, log_decay, beta, lengths};
@@ -247,15 +244,17 @@ la_status lin_attn_delta_forward(const la_delta_params* p, const void* q, const 
     return LA_ERR_INVALID_ARG;
   const size_t need = forward_bytes(*p);
   if ((st = check_delta_workspace(workspace, workspace_bytes, need)) != LA_OK) return st;
+  int* const flag = flag_of(workspace, workspace_bytes);
+  const size_t used = need ? need : flag ? sizeof(int) : 0;
   for (int i = 0; i < 6; ++i)
-    if (overlaps(workspace, need, in[i], nb[i])) return LA_ERR_INVALID_ARG;
-  if (overlaps(workspace, need, out, n.v) || overlaps(workspace, need, state, sbytes) ||
-      overlaps(workspace, need, state_out, sbytes))
+    if (overlaps(workspace, used, in[i], nb[i])) return LA_ERR_INVALID_ARG;
+  if (overlaps(workspace, used, out, n.v) || overlaps(workspace, used, state, sbytes) ||
+      overlaps(workspace, used, state_out, sbytes))
     return LA_ERR_INVALID_ARG;
   Args a = delta_args(*p, q, k, v, log_decay, beta, state, lengths);
   a.out = out;
   a.s1 = state_out;
-  a.flag = static_cast<int*>(workspace);
+  a.flag = flag;
   a.rec = static_cast<unsigned char*>(workspace) + LA_WORKSPACE_CONTROL_BYTES;
   return run_forward(a, p->B, p->dtype == LA_BF16, few_tokens(*p), cs);
 }

@@ -71,7 +71,7 @@ struct Args {
   float scale;
   int slices;            // slices of the value columns
   int chunks;            // chunks of N tokens
-  int* flag;             // workspace: its control block's flag word
+  int* flag;             // workspace: its control block's flag word, or null
   unsigned char* rec;    // records [B H][chunks]
   // the backward pass (delta_bwd.cu): per head and chunk an Image, that is planes
   // of the state before it, of the gradient of the state after it, of X and of

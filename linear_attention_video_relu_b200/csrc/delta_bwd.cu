@@ -1406,6 +1406,11 @@ la_status lin_attn_delta_backward(const la_delta_params* p, const void* dout, co
       if (overlaps(dq, n, in, n) || overlaps(dk, n, in, n)) return LA_ERR_INVALID_ARG;
     if (overlaps(dq, n, dk, n) || overlaps(dq, n, lengths, nl) || overlaps(dk, n, lengths, nl))
       return LA_ERR_INVALID_ARG;
+    int* const flag = flag_of(workspace, workspace_bytes);
+    for (const void* x : {(const void*)dq, (const void*)dk, q, k})
+      if (overlaps(flag, sizeof(int), x, n)) return LA_ERR_INVALID_ARG;
+    if (overlaps(flag, sizeof(int), lengths, nl)) return LA_ERR_INVALID_ARG;
+    if ((st = clear_flag(workspace, workspace_bytes, cs)) != LA_OK) return st;
     Args a = delta_args(*p, q, k, v, log_decay, beta, state, lengths);
     a.dq = dq;
     a.dk = dk;
@@ -1418,13 +1423,9 @@ la_status lin_attn_delta_backward(const la_delta_params* p, const void* dout, co
     return LA_ERR_INVALID_ARG;
   if (overlaps(dstate, sbytes, state, sbytes)) return LA_ERR_INVALID_ARG;
   if (p->N == 0) {
-    if (!dstate || dstate == dstate_out) return LA_OK;
-    const cudaError_t e =
-        dstate_out ? cudaMemcpyAsync(dstate, dstate_out, sbytes, cudaMemcpyDeviceToDevice, cs)
-                   : cudaMemsetAsync(dstate, 0, sbytes, cs);
-    if (e == cudaSuccess) return LA_OK;
-    cudaGetLastError();
-    return LA_ERR_CUDA;
+    if (overlaps(flag_of(workspace, workspace_bytes), sizeof(int), dstate, sbytes))
+      return LA_ERR_INVALID_ARG;
+    return copy_state(dstate, dstate_out, sbytes, workspace, workspace_bytes, cs);
   }
   const DeltaBytes n(*p);
   const BwdBytes ws(*p);

@@ -110,6 +110,32 @@ inline la_status check_delta_workspace(const void* ws, size_t bytes, size_t need
   return !ws || (uintptr_t)ws % 256 != 0 || bytes < need ? LA_ERR_WORKSPACE : LA_OK;
 }
 
+// The flag word of a workspace that a call is given, whether it needs it or not.
+inline int* flag_of(void* ws, size_t bytes) {
+  return aligned(ws, sizeof(int)) && bytes >= sizeof(int) ? static_cast<int*>(ws) : nullptr;
+}
+
+// Sets it to zero on `stream`, for calls whose kernels do not.
+inline la_status clear_flag(void* ws, size_t bytes, cudaStream_t stream) {
+  int* flag = flag_of(ws, bytes);
+  if (!flag || cudaMemsetAsync(flag, 0, sizeof(int), stream) == cudaSuccess) return LA_OK;
+  cudaGetLastError();
+  return LA_ERR_CUDA;
+}
+
+// `to` becomes `from` (or zeros), a call without tokens.
+inline la_status copy_state(float* to, const float* from, size_t bytes, void* ws, size_t ws_bytes,
+                            cudaStream_t stream) {
+  if (!to || to == from) return LA_OK;
+  const la_status st = clear_flag(ws, ws_bytes, stream);
+  if (st != LA_OK) return st;
+  const cudaError_t e = from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, stream)
+                             : cudaMemsetAsync(to, 0, bytes, stream);
+  if (e == cudaSuccess) return LA_OK;
+  cudaGetLastError();
+  return LA_ERR_CUDA;
+}
+
 // Checks that need no device.
 inline la_status check_delta(const la_delta_params* p) {
   if (!p) return LA_ERR_INVALID_ARG;

@@ -4,7 +4,7 @@ import pytest
 
 import __graft_entry__
 from linear_attention_video_relu_b200 import _native as C
-from test_delta_rotary_host import DK, DQ, K, LEN, Q, _backward, _delta, _forward
+from test_delta_rotary_host import DK, DQ, G, K, LEN, O, Q, S0, S1, V, _backward, _delta, _forward
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -22,3 +22,15 @@ def test_gradients_without_value_heads():
     assert _backward(_delta(H=0, Hk=2, N=0), dq=None) == C.LA_OK
     assert _backward(_delta(B=0), dq=None) == C.LA_OK
     assert _forward(p) == C.LA_OK
+
+
+@pytest.mark.parametrize("other", [Q, K, V, G, S0, O, S1, LEN])
+def test_the_flag_word_of_a_workspace_that_is_not_needed(other):
+    """It is written all the same, so it may lie in nothing else."""
+    p = _delta(N=1)
+    assert C.lin_attn_delta_workspace_size(p) == 0
+    assert _forward(p, workspace=other, workspace_bytes=4) == C.LA_ERR_INVALID_ARG
+    if other in (S1, Q):
+        z = _delta(N=0) if other == S1 else _delta(H=0, Hk=2)
+        f = _forward if other == S1 else _backward
+        assert f(z, workspace=other, workspace_bytes=4) == C.LA_ERR_INVALID_ARG

@@ -29,3 +29,32 @@ def test_gradients_without_value_heads(dtype, layout, lengths):
     live = live.expand(B, N)[:, None, :, None] if layout == "bhnd" else live.expand(B, N)[:, :, None, None]
     for a in out[:2]:
         assert torch.equal(a, torch.where(live, 0.0, 7.0).to(dtype).expand_as(a))
+
+
+def _inputs(B, H, N, D=64, dtype=torch.bfloat16):
+    q = torch.nn.functional.normalize(torch.randn(B, H, N, D, device="cuda"), dim=-1).to(dtype)
+    g = torch.zeros(B, H, N, device="cuda", dtype=dtype)
+    return q, q, q, g - 0.5, g + 0.5
+
+
+@pytest.mark.parametrize("flag", [-1, 8], ids=["junk", "set"])
+def test_a_status_is_that_of_the_last_call(flag):
+    """Whatever the flag word holds before, and whether the call needs a workspace."""
+    OK = la._native.LA_OK
+    few, many, chunks = _inputs(1, 2, 1), _inputs(16, 16, 20), _inputs(1, 2, 100)
+    S = torch.randn(1, 2, 64, 64, device="cuda")
+    nothing = [t[:, :, :0] for t in few]
+    no_heads = [few[0], few[1]] + [t[:, :0] for t in few[2:]]
+    p = la.api._delta_params(*chunks, None, "bhnd")
+    ws = la.Workspace(la._native.lin_attn_delta_backward_workspace_size(p), "cuda")
+    for call in (lambda: la.delta_forward(*few, workspace=ws), lambda: la.delta_forward(*many, workspace=ws),
+                 lambda: la.delta_forward(*chunks, workspace=ws),
+                 lambda: la.delta_forward(*nothing, state=S, workspace=ws),
+                 lambda: la.delta_forward(*nothing, workspace=ws),
+                 lambda: la.delta_backward(torch.ones_like(chunks[2]), *chunks, workspace=ws),
+                 lambda: la.delta_backward(torch.ones_like(few[2]), *few, workspace=ws),
+                 lambda: la.delta_backward(nothing[2], *nothing, state=S, dstate_out=S, workspace=ws),
+                 lambda: la.delta_backward(no_heads[2], *no_heads, workspace=ws)):
+        ws.buf.view(torch.int32)[:] = flag
+        call()
+        assert ws.status() == OK
