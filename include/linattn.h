@@ -345,7 +345,7 @@ typedef struct {
  * flag that lin_attn_device_status reports. A call that enqueues work sets it to
  * zero, where it is given a workspace but needs none too (then of any size from
  * one word): so it speaks of the last such call alone, and to know of every
- * call, ask after each.
+ * call, ask after each. What a wait that was given up leaves void is NaN.
  * N = 0: state_out becomes `state` (or zeros).
  * Errors (nothing launched): LA_ERR_INVALID_ARG for a size, width, dtype or
  * layout out of range, a missing or misaligned pointer (q, k, v, out and the

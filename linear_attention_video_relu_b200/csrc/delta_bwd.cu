@@ -192,6 +192,20 @@ __global__ void __launch_bounds__(256 + kLoadThreads, 1) reverse_kernel(const Ar
       }
     }
     if (sizeof(T) == 2) ptx::cp_async_wait_all();
+    if (!*gave_up) return;
+    // what this thread has stored is void
+    unsigned char* img = I::at(a, (long long)bh * a.chunks);
+    void_image<KD, PO, NV, KD>(img, I::offD, a.atoms, n0, chunks, tid);
+    void_image<KD, PO, NV, kC>(img, I::offR, a.atoms, n0, chunks, tid);
+    constexpr int V = NV / 8;
+    for (int c = 0; c < chunks; ++c)
+      for (int j = tid; j < kC * V; j += kLoadThreads) {
+        const int row = c * kC + j / V, c8 = j % V;
+        const float x[8] = {void_value(), void_value(), void_value(), void_value(),
+                            void_value(), void_value(), void_value(), void_value()};
+        if (row < len && n0 + c8 * 8 < a.Dv)
+          mm::Io<T>::store8(dvp + row * rv.stride + c8 * 8, x);
+      }
     return;
   }
 
@@ -297,6 +311,7 @@ __global__ void __launch_bounds__(256 + kLoadThreads, 1) reverse_kernel(const Ar
       if (i + NBUF < chunks) ptx::bar_arrive(kRevFree + buf, 256);
     }
     if (a.ds0) {
+      const bool bad = *gave_up;
 #pragma unroll
       for (int m = 0; m < MS; ++m)
 #pragma unroll
@@ -306,7 +321,8 @@ __global__ void __launch_bounds__(256 + kLoadThreads, 1) reverse_kernel(const Ar
             const int row = sh.state + 16 * m + r + 8 * i, col = n0 + nw + 8 * n + c2;
             if (row < a.D && col < a.Dv)
               *reinterpret_cast<float2*>(a.ds0 + s_at + (long long)row * a.Dv + col) =
-                  make_float2(S[m][n][2 * i], S[m][n][2 * i + 1]);
+                  bad ? make_float2(void_value(), void_value())
+                      : make_float2(S[m][n][2 * i], S[m][n][2 * i + 1]);
           }
     }
     // what follows takes this kernel's end for scan_kernel's, too
@@ -1138,9 +1154,12 @@ __global__ void __launch_bounds__(512, 1) gradient_tc_kernel(const Args a) {
     float* bDK = bDQ + Cfg::offDK / 4;
     float* bP = reinterpret_cast<float*>(smem + last + Cfg::offP) + i * Cfg::pitchC + 16 * cq;
     float* bA = bP + (Cfg::offA - Cfg::offP) / 4;
-    const float4 g = gates->tok[i];
+    float4 g = gates->tok[i];
+    const float bad = *gave_up ? void_value() : 0.f;   // a wait was given up
+    g.z += bad;   // dk
+    g.w += bad;   // dq
     const unsigned char* krow = smem + within + i * kLK + cq * NC * 2;
-    float py = 0.f, pz = 0.f, dk[NC];   // k . (dR S^T), k . (X dS'^T); z . X dS'^T - x . dR S^T
+    float py = bad, pz = 0.f, dk[NC];   // k . (dR S^T), k . (X dS'^T); z . X dS'^T - x . dR S^T
     {
       uint32_t ki[NC], ko[NC];
       ptx::tmem_ld_32x32(mine + (quad < 2 ? KD : 0) + cq * NC, ki);

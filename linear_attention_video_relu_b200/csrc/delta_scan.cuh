@@ -65,6 +65,15 @@ struct ScanCfg {
   static constexpr int threads = 256 + kLoadThreads;
 };
 
+// NaN for a thread's part of the outputs: the pairs of columns 0 and 8, of `cols`,
+// in rows row, row + 8 and so every 64.
+template <typename T>
+__device__ __noinline__ void void_rows(T* out, long long stride, int row, int rows, int cols) {
+  for (; row < rows; row += row & 8 ? kC - 8 : 8)
+    for (int n = 0; n < 16 && n < cols; n += 8)
+      mm::Io<T>::store2(out + row * stride + n, void_value(), void_value());
+}
+
 // BWD: instead of `out`, leave the state before every chunk and X in the
 // workspace for the backward pass.
 template <typename T, int KD, int RT, int PC, int PO, int NBUF, bool BWD>
@@ -237,6 +246,7 @@ __global__ void __launch_bounds__(256 + kLoadThreads, 1) scan_kernel(const Args 
       if (c + NBUF < chunks) ptx::bar_arrive(kBarFree + buf, 384);
     }
     if (a.s1) {
+      const bool bad = *gave_up;
 #pragma unroll
       for (int m = 0; m < MS; ++m)
 #pragma unroll
@@ -246,7 +256,8 @@ __global__ void __launch_bounds__(256 + kLoadThreads, 1) scan_kernel(const Args 
             const int row = sh.state + 16 * m + r + 8 * i, col = n0 + nw + 8 * n + c2;
             if (row < a.D && col < a.Dv)
               *reinterpret_cast<float2*>(a.s1 + s_at + (long long)row * a.Dv + col) =
-                  make_float2(S[m][n][2 * i], S[m][n][2 * i + 1]);
+                  bad ? make_float2(void_value(), void_value())
+                      : make_float2(S[m][n][2 * i], S[m][n][2 * i + 1]);
           }
     }
     return;
@@ -309,6 +320,18 @@ __global__ void __launch_bounds__(256 + kLoadThreads, 1) scan_kernel(const Args 
     if (c + 1 < chunks) ptx::bar_arrive(kBarRead, 256);
     if (c + NBUF < chunks) ptx::bar_arrive(kBarFree + buf, 384);
   }
+  if (!*gave_up) return;
+  // what this thread has stored is void
+  if (BWD) {
+    using I = Image<KD, PO>;
+    unsigned char* img = I::at(a, (long long)bh * a.chunks);
+    void_image<KD, PO, NV, KD>(img, I::offS, a.atoms, n0, chunks, tid);
+    void_image<KD, PO, NV, kC>(img, I::offX, a.atoms, n0, chunks, tid);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < RT; ++j)
+    void_rows(op, rv.stride, 16 * sh.tile[j] + r, len, a.Dv - (n0 + nw + c2));
 }
 
 }  // namespace delta

@@ -1,5 +1,9 @@
 """The gated delta rule's calls that the other tests leave out: no value heads,
 workspaces' status, long offsets."""
+import os
+import shutil
+import subprocess
+
 import pytest
 import torch
 
@@ -58,3 +62,16 @@ def test_a_status_is_that_of_the_last_call(flag):
         ws.buf.view(torch.int32)[:] = flag
         call()
         assert ws.status() == OK
+
+
+@pytest.mark.skipif(shutil.which("nvcc") is None, reason="needs nvcc")
+def test_a_wait_that_nothing_ends_gives_up(tmp_path):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = str(tmp_path / "wait_check")
+    subprocess.check_call(["nvcc", "-gencode", "arch=compute_100a,code=sm_100a", "-std=c++17", "-O2",
+                           "--expt-relaxed-constexpr", "-I",
+                           os.path.join(root, "linear_attention_video_relu_b200", "csrc"), "-I",
+                           os.path.join(root, "include"),
+                           os.path.join(root, "tests", "c", "wait_check.cu"), "-o", exe])
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout + r.stderr
