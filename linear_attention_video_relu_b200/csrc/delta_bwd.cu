@@ -390,34 +390,36 @@ __global__ void __launch_bounds__(256 + kLoadThreads, 1) reverse_kernel(const Ar
   }
 }
 
-// ---- a chunk's gradients ---------------------------------------------------------------
+// ---- a chunk's gradients in fp32 ---------------------------------------------------------
 //
 // One CTA of sixteen warps per (chunk, head). Warp (m, ch) has rows 16 m of the
 // chunk, a quarter of the key columns of dq and dk, and block (m, ch) of the
 // products within the chunk. The products with S and dS' run over the value
-// columns in slices of NV, the next slice's copies under way meanwhile (NBUF 2);
-// then the products within the chunk follow from EP and F in shared memory.
-// What it has to read is mostly S and dS' (8 D Dv bytes a chunk in two planes
-// each, where q, k, v and their gradients are 2 (4 D + 3 Dv) 64); what it waits
-// for is the latency of its own chain of small products, hence the many warps.
-// CTAs go by chunks, then heads: the first chunks' dS' and dR were written last
-// and are in the L2 still (1 to 2 % of a backward call).
+// columns in slices of NV, one after another (K and Q of three planes leave no
+// room for a second slice); then the products within the chunk follow from EP and
+// F in shared memory. What it has to read is mostly S and dS' (12 D Dv bytes a
+// chunk in three planes each, and 768 Dv of X and dR, where q, k, v, dout and the
+// gradients are 4 (4 D + 3 Dv) 64); what it waits for is the latency of its own
+// chain of small products, hence the many warps. CTAs go by chunks, then heads:
+// the first chunks' dS' and dR were written last and are in the L2 still (of a
+// call of three heads of 333 tokens 69 us became 66).
 constexpr int kSums = 25 * kC + 16;   // floats: the sums that a chunk's dbeta and dg are made of
 
-template <typename T, int KD, int NV, int PO, int NBUF>
+template <int KD, int NV, int PO>
 struct GradCfg {
+  using T = float;
   static constexpr int PI = mm::Io<T>::kPlanes;
   static constexpr int kLK = (KD + 8) * 2, kPlaneK = kC * kLK;
   static constexpr int kLN = (NV + 8) * 2, kPlaneS = KD * kLN, kPlaneX = kC * kLN;
   static constexpr int offK = 0, offQ = PI * kPlaneK, offStage = 2 * PI * kPlaneK;
-  // a stage: S, dS', dO, X, dR, and V as it is
+  // a slice: S, dS', dO, X, dR, and V as it is
   static constexpr int offS = 0, offD = PO * kPlaneS, offO = 2 * PO * kPlaneS;
   static constexpr int offX = offO + PI * kPlaneX, offR = offX + PO * kPlaneX;
   static constexpr int offV = offR + PO * kPlaneX;
   static constexpr int stage = offV + kC * NV * (int)sizeof(T);
-  // EP and F take the stages' place
+  // EP and F take its place
   static constexpr int tri = 2 * PO * mm::kTriPlane;
-  static constexpr int offGate = offStage + (NBUF * stage > tri ? NBUF * stage : tri);
+  static constexpr int offGate = offStage + (stage > tri ? stage : tri);
   static constexpr int offDec = offGate + (int)sizeof(Gates);
   static constexpr int offSum = offDec + (int)sizeof(Decays);
   static constexpr int bytes = offSum + kSums * 4;
@@ -715,11 +717,12 @@ __device__ __forceinline__ void finish(const Args& a, const Within& x, int bh, i
   }
 }
 
-template <typename T, int KD, int NV, int PC, int PO, int NBUF>
+template <int KD, int NV, int PC, int PO>
 __global__ void __launch_bounds__(512, 1) gradient_kernel(const Args a) {
   ptx::launch_dependents();
   ptx::grid_dependency_wait();
-  using Cfg = GradCfg<T, KD, NV, PO, NBUF>;
+  using T = float;
+  using Cfg = GradCfg<KD, NV, PO>;
   using Rec = Record<PC, PC>;
   constexpr int kT = Cfg::threads;
   constexpr bool kApart = Cfg::PI == 3;
@@ -741,7 +744,7 @@ __global__ void __launch_bounds__(512, 1) gradient_kernel(const Args a) {
   using I = Image<KD, PO>;
   const unsigned char* img = I::at(a, at);
   auto load_slice = [&](int s) {
-    const uint32_t st = sbase + Cfg::offStage + (s % NBUF) * Cfg::stage;
+    const uint32_t st = sbase + Cfg::offStage;
     const int n0 = s * NV;
     // rows of NV columns out of the image's tiles: all within one atom
     auto load_image = [&](int dst, int plane, int tile, int rows_in_tile) {
@@ -791,9 +794,8 @@ __global__ void __launch_bounds__(512, 1) gradient_kernel(const Args a) {
   for (int s = 0; s < slices; ++s) {
     ptx::cp_async_wait_all();
     __syncthreads();
-    if (NBUF > 1 && s + 1 < slices) load_slice(s + 1);
-    const uint32_t st = sbase + Cfg::offStage + (s % NBUF) * Cfg::stage;
-    const unsigned char* stp = smem + Cfg::offStage + (s % NBUF) * Cfg::stage;
+    const uint32_t st = sbase + Cfg::offStage;
+    const unsigned char* stp = smem + Cfg::offStage;
     const mm::Operand aO = mm::a_tile<false>(st + Cfg::offO + 16 * m * kLN, kLN, Cfg::kPlaneX);
     const mm::Operand aX = mm::a_tile<false>(st + Cfg::offX + 16 * m * kLN, kLN, Cfg::kPlaneX);
     const mm::Operand aR = mm::a_tile<false>(st + Cfg::offR + 16 * m * kLN, kLN, Cfg::kPlaneX);
@@ -840,12 +842,9 @@ __global__ void __launch_bounds__(512, 1) gradient_kernel(const Args a) {
       }
       ss += x * u + y * v;
     }
-    if (NBUF == 1) {
-      __syncthreads();
-      if (s + 1 < slices) load_slice(s + 1);
-    }
+    __syncthreads();   // the slice's place is free
+    if (s + 1 < slices) load_slice(s + 1);
   }
-  __syncthreads();   // the stages' place is free
 
   const Gates* gates = reinterpret_cast<const Gates*>(smem + Cfg::offGate);
   const Decays* dec = reinterpret_cast<const Decays*>(smem + Cfg::offDec);
@@ -1354,7 +1353,8 @@ la_status run_shared_heads(const Args& a, bool next, cudaStream_t stream) {
   return launch<shared_heads_kernel<T>>((unsigned)((count + 255) / 256), 256, 0, stream, a, next);
 }
 
-template <typename T, int KD, int RT, int PC, int NBUF, int GNV = 16>
+// GNV: value columns to a slice of gradient_kernel (fp32 only).
+template <typename T, int KD, int RT, int PC, int NBUF, int GNV = 0>
 la_status run_backward(Args a, int B, cudaStream_t stream) {
   constexpr int PO = grad_planes<T>();
   const long long heads = (long long)B * a.H;
@@ -1382,8 +1382,8 @@ la_status run_backward(Args a, int B, cudaStream_t stream) {
     }
     st = launch<gradient_tc_kernel<KD, PC>>(grid, Grad::threads, Grad::bytes, stream, a, true);
   } else {
-    using Grad = GradCfg<T, KD, GNV, PO, 1>;
-    st = launch<gradient_kernel<T, KD, GNV, PC, PO, 1>>(each, Grad::threads, Grad::bytes, stream, a, true);
+    using Grad = GradCfg<KD, GNV, PO>;
+    st = launch<gradient_kernel<KD, GNV, PC, PO>>(each, Grad::threads, Grad::bytes, stream, a, true);
   }
   if (st != LA_OK || a.Hk == a.H) return st;
   return run_shared_heads<T>(a, true, stream);
