@@ -46,7 +46,7 @@ struct Args {
   int tokens;             // B N
   int per_thread;         // heads per thread
   float amplitude, sign;
-  uint64_t freq[kMaxPairs]; // whole turns per position, less whole ones, in 2^-64
+  uint64_t freq[kMaxPairs]; // turns per position, less whole ones, in 2^-64
 };
 
 template <typename T>
@@ -120,9 +120,12 @@ __device__ __forceinline__ int position(const Args& a, int axis, int b, int n) {
 }
 
 // cos and sin of pair `m` at position `pos`. The angle is kept in 2^-64 turns,
-// where whole turns fall off a 64-bit product by themselves and what is left is
-// off by pos 2^-65 turns: exact where fp32 and its range reduction would not be.
-// The upper 32 bits, as a signed number of 2^-31 half turns, go to sincospi.
+// where whole turns fall off a 64-bit product by themselves and nothing is rounded:
+// what is left is off by the frequency's own error times pos. The frequencies are
+// made in 64-bit floating point, up to 2^-55 turns off, so an angle is off by less
+// than 2^-24 turns (3e-7 radians, an fp32 rounding) at every position of 32 bits,
+// where an fp32 product would lose whole turns. The upper 32 bits, as a signed
+// number of 2^-31 half turns, go to sincospi.
 __device__ __forceinline__ void turn(const Args& a, int m, int pos, float* c, float* s) {
   const uint64_t x = (uint64_t)(int64_t)pos * a.freq[m];
   float sn, cs;
