@@ -322,16 +322,16 @@ __global__ void __launch_bounds__(256 + kLoadThreads, 1) scan_kernel(const Args 
   }
   if (!*gave_up) return;
   // what this thread has stored is void
-  if (BWD) {
+  if constexpr (BWD) {
     using I = Image<KD, PO>;
     unsigned char* img = I::at(a, (long long)bh * a.chunks);
     void_image<KD, PO, NV, KD>(img, I::offS, a.atoms, n0, chunks, tid);
     void_image<KD, PO, NV, kC>(img, I::offX, a.atoms, n0, chunks, tid);
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int j = 0; j < RT; ++j)
-    void_rows(op, rv.stride, 16 * sh.tile[j] + r, len, a.Dv - (n0 + nw + c2));
+    for (int j = 0; j < RT; ++j)
+      void_rows(op, rv.stride, 16 * sh.tile[j] + r, len, a.Dv - (n0 + nw + c2));
+  }
 }
 
 }  // namespace delta
