@@ -343,9 +343,10 @@ typedef struct {
  * workspace: lin_attn_delta_workspace_size bytes, 256-byte aligned (NULL will do
  * where that is 0). It may hold anything and is clobbered; its first word is the
  * flag that lin_attn_device_status reports. A call that enqueues work sets it to
- * zero, where it is given a workspace but needs none too (then of any size from
- * one word): so it speaks of the last such call alone, and to know of every
- * call, ask after each. What a wait that was given up leaves void is NaN.
+ * zero, also where it needs no workspace but is given one of at least
+ * LA_WORKSPACE_CONTROL_BYTES: so it speaks of the last such call alone, and to
+ * know of every call, ask after each. What a wait that was given up leaves void
+ * is NaN.
  * N = 0: state_out becomes `state` (or zeros).
  * Errors (nothing launched): LA_ERR_INVALID_ARG for a size, width, dtype or
  * layout out of range, a missing or misaligned pointer (q, k, v, out and the

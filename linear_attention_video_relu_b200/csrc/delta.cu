@@ -227,7 +227,8 @@ la_status lin_attn_delta_forward(const la_delta_params* p, const void* q, const 
     return LA_ERR_INVALID_ARG;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (p->N == 0) {
-    if (overlaps(flag_of(workspace, workspace_bytes), sizeof(int), state_out, sbytes))
+    const int* flag = flag_of(workspace, workspace_bytes);
+    if (overlaps(flag, sizeof(int), state, sbytes) || overlaps(flag, sizeof(int), state_out, sbytes))
       return LA_ERR_INVALID_ARG;
     return copy_state(state_out, state, sbytes, workspace, workspace_bytes, cs);
   }

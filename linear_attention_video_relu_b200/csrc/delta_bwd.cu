@@ -1442,7 +1442,8 @@ la_status lin_attn_delta_backward(const la_delta_params* p, const void* dout, co
     return LA_ERR_INVALID_ARG;
   if (overlaps(dstate, sbytes, state, sbytes)) return LA_ERR_INVALID_ARG;
   if (p->N == 0) {
-    if (overlaps(flag_of(workspace, workspace_bytes), sizeof(int), dstate, sbytes))
+    const int* flag = flag_of(workspace, workspace_bytes);
+    if (overlaps(flag, sizeof(int), dstate_out, sbytes) || overlaps(flag, sizeof(int), dstate, sbytes))
       return LA_ERR_INVALID_ARG;
     return copy_state(dstate, dstate_out, sbytes, workspace, workspace_bytes, cs);
   }

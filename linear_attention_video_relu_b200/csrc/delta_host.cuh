@@ -110,9 +110,11 @@ inline la_status check_delta_workspace(const void* ws, size_t bytes, size_t need
   return !ws || (uintptr_t)ws % 256 != 0 || bytes < need ? LA_ERR_WORKSPACE : LA_OK;
 }
 
-// The flag word of a workspace that a call is given, whether it needs it or not.
+// The flag word of a workspace that a call is given, whether it needs it or not: of
+// one with a control block, which is what lin_attn_device_status reads and clears.
 inline int* flag_of(void* ws, size_t bytes) {
-  return aligned(ws, sizeof(int)) && bytes >= sizeof(int) ? static_cast<int*>(ws) : nullptr;
+  return aligned(ws, sizeof(int)) && bytes >= LA_WORKSPACE_CONTROL_BYTES ? static_cast<int*>(ws)
+                                                                         : nullptr;
 }
 
 // Sets it to zero on `stream`, for calls whose kernels do not.

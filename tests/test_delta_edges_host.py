@@ -24,13 +24,22 @@ def test_gradients_without_value_heads():
     assert _forward(p) == C.LA_OK
 
 
+BLOCK = C.LA_WORKSPACE_CONTROL_BYTES
+
+
 @pytest.mark.parametrize("other", [Q, K, V, G, S0, O, S1, LEN])
 def test_the_flag_word_of_a_workspace_that_is_not_needed(other):
     """It is written all the same, so it may lie in nothing else."""
     p = _delta(N=1)
     assert C.lin_attn_delta_workspace_size(p) == 0
-    assert _forward(p, workspace=other, workspace_bytes=4) == C.LA_ERR_INVALID_ARG
-    if other in (S1, Q):
-        z = _delta(N=0) if other == S1 else _delta(H=0, Hk=2)
-        f = _forward if other == S1 else _backward
-        assert f(z, workspace=other, workspace_bytes=4) == C.LA_ERR_INVALID_ARG
+    assert _forward(p, workspace=other, workspace_bytes=BLOCK) == C.LA_ERR_INVALID_ARG
+
+
+def test_the_flag_word_of_calls_without_tokens_or_value_heads():
+    for ws in (S0, S1):
+        assert _forward(_delta(N=0), workspace=ws, workspace_bytes=BLOCK) == C.LA_ERR_INVALID_ARG
+        assert _backward(_delta(N=0), dstate_out=S0, workspace=ws,
+                         workspace_bytes=BLOCK) == C.LA_ERR_INVALID_ARG
+    for ws in (Q, K, DQ, DK, LEN):
+        assert _backward(_delta(H=0, Hk=2), workspace=ws,
+                         workspace_bytes=BLOCK) == C.LA_ERR_INVALID_ARG

@@ -64,6 +64,13 @@ def test_a_status_is_that_of_the_last_call(flag):
         assert ws.status() == OK
 
 
+def test_a_workspace_without_a_control_block_is_left_alone():
+    ws = la.Workspace(256, "cuda")
+    ws.buf.fill_(255)
+    la.delta_forward(*_inputs(1, 2, 1), workspace=ws)
+    assert (ws.buf == 255).all()
+
+
 @pytest.mark.skipif(shutil.which("nvcc") is None, reason="needs nvcc")
 def test_a_wait_that_nothing_ends_gives_up(tmp_path):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
