@@ -337,7 +337,8 @@ typedef struct {
  *              What lies behind them is not read, and those rows of `out` are
  *              left as they were.
  * A log_decay below -100 (-inf too) counts as -100. The state is carried in
- * fp32, and the operands of the tensor cores keep all its bits.
+ * fp32, and the operands of the tensor cores keep all its bits, for `out` too,
+ * which is rounded to dtype once.
  * An infinity or NaN in a token that is read may reach all outputs of its chunk,
  * those of earlier tokens too, and what follows; other heads never.
  * workspace: lin_attn_delta_workspace_size bytes, 256-byte aligned (NULL will do
@@ -370,8 +371,18 @@ LA_API la_status lin_attn_delta_workspace_size(const la_delta_params* p, size_t*
  * nothing has to be kept from the forward call. dq and dk of a shared head are
  * the sums over its value heads. Rows behind lengths[b] are not read, and are
  * left as they were in the gradients. A log_decay of -100 or below gets the
- * gradient of one of -100. The results do not depend on the order in which
- * CTAs run. Arguments otherwise, and errors, as in lin_attn_delta_forward;
+ * gradient of one of -100. dlog_decay is a sum of terms that all have
+ * exp(log_decay) in them, so strong decays' small gradients have digits of their
+ * own. The results do not depend on the order in which CTAs run.
+ * Rounding: fp32 calls and dstate keep all bits of fp32 up to their sums. The
+ * gradients in bf16 are made from operands of 17 bits on the tensor cores (sums
+ * and carried states are fp32) and rounded once: 0.5 to 0.8 % of them are not the
+ * exact value's rounding, 0.02 to 0.05 % in an fp32 computation. Where dstate is
+ * NULL the chains take 17 bits as well, so whether it is asked for may change
+ * the last bit of the others.
+ * The workspace holds S, dS', X and dR of every chunk of 64 tokens: 2 x 16 heads
+ * of 4096 tokens, 128 x 128 (Hk 8) 605 MB; 32 heads of 32,760 tokens 1.6 GB at 64
+ * x 64, 3.8 GB at 128 x 128 (the forward call's 0.55 GB). Arguments otherwise, and errors, as in lin_attn_delta_forward;
  * dout, dq, dk, dv, dstate_out and dstate are 16-byte aligned.
  * workspace: lin_attn_delta_backward_workspace_size bytes, 256-byte aligned. */
 LA_API la_status lin_attn_delta_backward(const la_delta_params* p, const void* dout,

@@ -422,7 +422,9 @@ def delta_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: 
     behind them are left as they were, and zero in an `out` made here. scale:
     D ** -0.5 unless given. workspace: at least lin_attn_delta_workspace_size
     bytes, made here unless given. stream: the call's, for what it makes too.
-    Keys are taken as they are: normalise them first."""
+    Keys are taken as they are: normalise them first. The results are in no
+    autograd graph, whatever q, k and the others require: delta_backward gives
+    the gradients, to a torch.autograd.Function or to whoever calls it."""
     p = _delta_params(q, k, v, log_decay, beta, scale, layout)
     dev = q.get_device()
     with _on_stream(q, stream):
@@ -459,8 +461,10 @@ def delta_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torc
 
     out: five tensors to take dq, dk, dv, dlog_decay and dbeta; with lengths,
     rows behind them are left as they were there, and zero in tensors made
-    here. dstate may be dstate_out itself. workspace: at least
-    lin_attn_delta_backward_workspace_size bytes, made here unless given."""
+    here. dstate may be dstate_out itself; whether it is wanted may change the last
+    bit of the other gradients in bf16 (linattn.h). workspace: at least
+    lin_attn_delta_backward_workspace_size bytes (0.6 GB for 2 x 16 heads of 4096
+    tokens, 128 x 128), made here unless given."""
     p = _delta_params(q, k, v, log_decay, beta, scale, layout)
     dev = q.get_device()
     _check_tensor(dout, v.shape, v.dtype, dev, "dout")
@@ -530,7 +534,8 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor] = None, *,
     row and column in three segments of the columns. style: "interleaved"
     (pairs 2m, 2m + 1) or "half" (m, m + dim / 2). scaling: "none", "linear",
     "ntk" or "by_parts" (with original_length, low, high turns), by `factor`.
-    amplitude multiplies the rotated columns. out, k_out may be q and k."""
+    amplitude multiplies the rotated columns. out, k_out may be q and k. The
+    results are in no autograd graph: rotary_backward gives the gradients."""
     return _rotary(q, k, positions, offset, grid, rope_split, dim, style, theta, scaling, factor,
                    original_length, low, high, amplitude, out, k_out, stream, layout, 0)
 

@@ -24,7 +24,8 @@ namespace {
 // one pass over the rows gives S^T k, S^T q and k.q, and a token costs one
 // reduction: two shuffles, then four warps' sums through shared memory. 64
 // sequences of 32 heads of 128 x 128 (270 MB) take 43 us, 6.2 TB/s; one of 64 x
-// 64 takes 4.4, the latency of its loads and of the reduction. (Loading the next
+// 64 takes 4.4 with cold caches and 2.7 in a loop that is replayed, its launch and
+// the latency of its loads and of the reduction. (Loading the next
 // CTA's rows ahead was slower: fewer CTAs share an SM.)
 constexpr int kStepCols = 32, kStepThreads = 128;
 
@@ -163,10 +164,10 @@ la_status run_chunks(Args a, int B, cudaStream_t stream) {
 }
 
 // One after another or in chunks: a token takes 0.4 us where its CTAs fit the
-// device at once, the two kernels for chunks 10 to 12 us at few heads whatever
-// the tokens, so they are even at about 19 tokens (8 heads, D 64 and 128). With
-// many heads the chunks' CTAs, one per SM, queue: 256 heads of D 128, 20 tokens:
-// 36 against 43 us; 1024 of D 64: 49 against 101.
+// device at once, the two kernels for chunks 10.4 to 12.5 us at few heads whatever
+// the tokens, so they are even at 17 (8 heads of D 128) to 20 tokens (D 64, and 32
+// heads of D 128). With many heads the chunks' CTAs, one per SM, queue: 256 heads
+// of D 128, 24 tokens: 42 against 45 us; 1024 of D 64: 58 against 73.
 bool few_tokens(const la_delta_params& p) {
   const long long chains = (long long)p.B * p.H * ((p.Dv + 15) / 16);
   return p.N <= LA_DELTA_STEP_TOKENS || (p.N <= 24 && chains > 512);

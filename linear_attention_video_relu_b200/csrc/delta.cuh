@@ -251,11 +251,12 @@ __device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, int* f
 }
 
 // The sequence that the chains of rank `n` work on: the n-th longest, so that
-// the last CTAs to start are short ones. Batches of random lengths, forward: 8
-// sequences of up to 4096 tokens, 16 heads of D 128: 440 us in the order given,
-// 351 so (lucky orders: 420 and 425); 16 of up to 2048, D 64: 210 and 179; 64 of
-// up to 1024, whose order matters least: 475 and 469 to 480 and 486. All threads
-// of a CTA call, and meet here; `found` is shared by them.
+// the last CTAs to start are short ones. Batches of random lengths, 16 heads,
+// forward, five draws each in the order given and so: 8 sequences of up to 4096
+// tokens of D 128: 449 and 426 us on average (526 and 451, 393 and 364 at best, 547
+// and 551 at worst); 16 of up to 2048, D 64: 218 and 210; 64 of up to 1024, D 128,
+// whose order matters least: 955 and 964. All threads of a CTA call, and meet
+// here; `found` is shared by them.
 constexpr int kRanked = 128;   // sequences: a thread compares its own with all
 __device__ __forceinline__ int nth_longest(const Args& a, int n, volatile int* found) {
   const int t = threadIdx.x;
@@ -316,15 +317,16 @@ struct Share {
 //
 // One CTA of four warps per (chunk, head): small, so that several share an SM
 // and hide one another's latencies (alone a CTA takes 9,100 cycles at D 64).
-// 16,384 chunks of D 64 take 208 us, half of it what their 690 MB would at the
-// measured bandwidth. What bounds it is the work on single elements, the decays
-// and the splits into planes: instruction issue is 52 % busy, shared memory 53 %,
-// the tensor pipe 22 %. Without P's stores it would take 8 % less, without the
-// diagonal blocks' inversion 6 %, without T's stores 4 %.
+// 16,384 chunks of D 64 take 220 us, of which their 814 MB (q and k once, the
+// records written) would be 124 at the measured bandwidth. What bounds it is the
+// work on single elements, the decays and the splits into planes: instruction issue
+// is 52 % busy, shared memory 56 %, the tensor pipe 21 %. With two planes of P, at
+// 208 us, P's stores were 8 % of it, the diagonal blocks' inversion 6 %, T's stores
+// 4 %.
 //
 // A long sequence in parts, the next part's T and P made beside the chains of
-// the last, gained nothing (1004 and 1005 us a call): the chains slow down by
-// as much.
+// the last, gained nothing (1004 and 1005 us a call, with two planes of P): the
+// chains slow down by as much.
 //
 // Warps 1 and 3 make the decays while 0 and 2 begin with the products, and have
 // fewer of the ten blocks in turn. T = (I + A)^-1 by 16 x 16 blocks: each warp

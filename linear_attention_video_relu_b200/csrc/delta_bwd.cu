@@ -20,7 +20,19 @@
 // Nothing is kept from the forward pass: the states before the chunks are made
 // again (scan_kernel), then the gradients of the states are carried backwards
 // (reverse_kernel), and with both in the workspace all chunks' gradients are
-// made at once (gradient_kernel).
+// made at once (gradient_tc_kernel in bf16, gradient_kernel in fp32).
+//
+// Rounding: sums, and the two states that are carried, are fp32, and fp32 calls
+// keep all its bits in every product. In bf16 the operands that only gradients in
+// bf16 come from are two bf16 planes, 17 bits: S, dS', X, dR, EP and F, and where
+// no gradient of the initial state (fp32) is asked for the chains' T, R, dX too. Of
+// such gradients 0.5 to 0.8 % are not the exact value's rounding, where an fp32
+// computation has 0.02 to 0.05 %; their distance to the exact values is that of the
+// last rounding both ways (1.66e-3). With three planes everywhere the batch of
+// 2 x 16 heads of 4096 tokens, D 128, took 1088 us instead of 606: two atoms of
+// three planes of S and dS' are more than an SM's shared memory, so that the
+// products fell to warp-level instructions, and chains of 32 columns do not fit
+// either.
 #include "linattn.h"
 
 #include "delta_host.cuh"
@@ -926,7 +938,8 @@ __global__ void __launch_bounds__(512, 1) gradient_kernel(const Args a) {
 // of 23,000 cycles at D = 128 3,000 wait for the first atom, 7,000 are the two
 // atoms' products and copies, 3,000 the way out of tensor memory, 2,000
 // make_within and 5,500 finish (32 heads of 4096 tokens: 227 us, of which the
-// 256 KB a chunk are 85 at the measured bandwidth). A cluster per group of
+// 256 KB a chunk are 85 at the measured bandwidth; 237 with dlog_decay's rectangles
+// of pairs, which came later). A cluster per group of
 // shared heads that adds dq and dk up through its shared memory, instead of
 // shared_heads_kernel (27 us), was slower: 653 us a call against 646 with two
 // heads to a group, 773 against 636 with eight.
@@ -1331,6 +1344,8 @@ __global__ void __launch_bounds__(256) shared_heads_kernel(const Args a) {
 
 // ---- host --------------------------------------------------------------------------------
 
+// (A record has room for three planes of T and of P, which calls that want dstate
+// fill: whether one does is not known where the size is asked for.)
 struct BwdBytes {
   size_t rec, img, wdq, total;
   int atoms;
@@ -1493,9 +1508,10 @@ la_status lin_attn_delta_backward(const la_delta_params* p, const void* dout, co
   // the two kernels' chains run side by side
   bool wide = false;
   if ((st = wide_chains(2 * heads, p->Dv, &wide)) != LA_OK) return st;
-  // Gradients in bf16 need no more of the chains than 17 bits; that of the
-  // initial state, in fp32, needs all: three planes, which at D 128 leave no room
-  // for 32 columns.
+  // Gradients in bf16 take 17 bits of the chains (see the top); that of the initial
+  // state, in fp32, needs all: three planes, which at D 128 leave no room for 32
+  // columns (2 x 16 heads of 4096 tokens: 609 us without, 780 with; D 64: 315 and
+  // 351).
   if (dstate) {
     if (p->D > 64) return run_backward<bf16, 128, 1, 3, 2>(a, B, cs);
     return wide ? run_backward<bf16, 64, 2, 3, 2>(a, B, cs)

@@ -74,14 +74,16 @@ inline la_status device_sms(int* sms) {
 }
 
 // Whether chains take 32 value columns per CTA and not 16 (RT 2 and 1 of the
-// chains' kernels). 32 columns cost 1.25 to 1.45 times as long as 16, so they win
+// chains' kernels). 32 columns cost 1.2 to 1.45 times as long as 16, so they win
 // where 16 would leave the device's SMs more than 1.4 times as many rounds of
-// CTAs, one per SM. 2048 tokens of D 128, forward: 16 heads 72 us with 16, 98
-// with 32; 24 heads 134 and 107; 40 heads 201 and 199; 128 heads 476 and 415.
-// D 64: 32 heads 66 and 83, 40 heads 115 and 86, 80 heads 177 and 164, 128 heads
-// 243 and 185. Backward, whose two kernels' chains run side by side, D 128: 8
-// heads 97 and 137, 16 heads 174 and 180, 36 heads 342 and 306, 128 heads 1160
-// and 1046; D 64: 40 heads 219 and 212, 128 heads 576 and 512.
+// CTAs, one per SM. 2048 tokens of D 128, forward: 16 heads 74 us with 16, 107
+// with 32; 24 heads 142 and 115; 40 heads (3 rounds and 2) 213 and 220; 64 heads
+// 290 and 234; 128 heads 507 and 457. D 64: 32 heads 67 and 90, 40 heads 119 and
+// 93, 80 heads 182 and 180, 128 heads 252 and 201. Backward, the CTAs of both
+// kernels' chains counted together, since the second kernel's start on what SMs
+// the first's leave, D 128: 8 heads 102 and 138, 16 heads 173 and 179, 20 heads (3
+// and 2) 244 and 252, 36 heads 344 and 309, 128 heads 1169 and 1060; D 64: 16 heads
+// 98 and 117, 40 heads 222 and 215, 128 heads 586 and 524.
 inline la_status wide_chains(long long heads, int Dv, bool* wide) {
   int sms = 0;
   const la_status st = device_sms(&sms);

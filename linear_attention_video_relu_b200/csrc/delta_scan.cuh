@@ -11,11 +11,11 @@
 //   warps 8-11   copies of the next chunks' K, Q, V and record.
 //
 // What bounds it is the chain's latency: at D 64 and 16 columns a chunk takes
-// 1.44 us (32 heads of 32,760 tokens: 737 us), of which the matrix instructions
+// 1.53 us (32 heads of 32,760 tokens: 781 us), of which the matrix instructions
 // of the busiest warp are 0.4; the rest are three splits into planes, four
-// barriers and the operands' way through shared memory, whose pipe is 60 % busy
-// (tensor 34 %, instruction issue 29 %). With 32 columns of D 128 (48 heads) it
-// is 69 % and the tensor pipe 57 %. The products are warp-level: one takes 21
+// barriers and the operands' way through shared memory, whose pipe is 64 % busy
+// (tensor 38 %, instruction issue 30 %). With 32 columns of D 128 (48 heads) it
+// is 67 % and the tensor pipe 59 %. The products are warp-level: one takes 21
 // cycles from operands to sums in registers, where a tcgen05 product has to be
 // committed, waited for and read back from tensor memory before the next step
 // of the chain can begin, and its operands, three planes of 128 x 128 state,
@@ -26,8 +26,9 @@
 // three, all bits of fp32, so neither the carried state nor `out` loses anything
 // to the tensor cores: of outputs in bf16 0.012 % are not the rounding of the
 // exact value, as of an fp32 computation (four heads of 1024 tokens, D 64). With
-// PO = 2, 17 bits, that is 0.76 %, for 6 to 9 % less time (480p clip 930 us
-// and 992, ragged batch 577 and 629, D 112 block 171 and 181).
+// PO = 2, 17 bits, that is 0.76 %, for 5 to 9 % less time (480p clip 930 us
+// and 982, ragged batch 577 and 630, D 112 block 171 and 181). The backward pass'
+// choice is in delta_bwd.cu.
 #pragma once
 
 #include "delta.cuh"
