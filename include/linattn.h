@@ -382,8 +382,9 @@ LA_API la_status lin_attn_delta_workspace_size(const la_delta_params* p, size_t*
  * the last bit of the others.
  * The workspace holds S, dS', X and dR of every chunk of 64 tokens: 2 x 16 heads
  * of 4096 tokens, 128 x 128 (Hk 8) 605 MB; 32 heads of 32,760 tokens 1.6 GB at 64
- * x 64, 3.8 GB at 128 x 128 (the forward call's 0.55 GB). Arguments otherwise, and errors, as in lin_attn_delta_forward;
- * dout, dq, dk, dv, dstate_out and dstate are 16-byte aligned.
+ * x 64, 3.8 GB at 128 x 128 (the forward call's 0.55 GB).
+ * Arguments otherwise, and errors, as in lin_attn_delta_forward; dout, dq, dk,
+ * dv, dstate_out and dstate are 16-byte aligned.
  * workspace: lin_attn_delta_backward_workspace_size bytes, 256-byte aligned. */
 LA_API la_status lin_attn_delta_backward(const la_delta_params* p, const void* dout,
                                          const void* q, const void* k, const void* v,
